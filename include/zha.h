@@ -458,10 +458,11 @@ int zha_lse_combine(int n_parts, long long walks, int d, const float *outs, cons
 /*
  * zha_reserve: allocate the search and attend scratch for up to max_walks walks
  * and selections of up to max_sel chunks now, so that later calls with at most
- * these sizes allocate nothing (e.g. before capturing them in a CUDA graph). A
- * captured call that would have to allocate is refused (ZHA_ERR_INVALID); once a
- * call has been captured, scratch that a larger call outgrows is kept until
- * zha_destroy, so that the graph stays replayable.
+ * these sizes allocate nothing (e.g. before capturing them in a CUDA graph).
+ * Every call that takes scratch: captured, it is refused (ZHA_ERR_INVALID, the
+ * capture goes on) if it would have to allocate, whatever the capture's mode; and
+ * scratch that it used is kept until zha_destroy when a larger call outgrows it, so
+ * that the graph stays replayable.
  */
 int zha_reserve(zha_tree *tree, long long max_walks, int max_sel);
 

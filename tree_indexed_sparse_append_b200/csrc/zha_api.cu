@@ -118,7 +118,7 @@ __global__ void count_bits_kernel(const unsigned *bits, long long words, unsigne
 
 }  // namespace
 
-// A scratch block outgrown after a call was captured.
+// A scratch block that a captured call used, outgrown since.
 struct zha_retired {
     void *block;
     zha_retired *next;
@@ -175,40 +175,46 @@ void probe_end(const zha_tree *t, int kind, cudaStream_t st) {
     cudaEventRecord(p->live.back().b, st);
 }
 
-void note_capture(zha_tree *t, cudaStream_t st) {
+bool is_captured(cudaStream_t st) {
     cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) cudaGetLastError();
-    t->capturing = s == cudaStreamCaptureStatusActive;
-    t->captured |= t->capturing;
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {  // the default stream beside another stream's capture
+        cudaGetLastError();
+        return false;
+    }
+    return s == cudaStreamCaptureStatusActive;
 }
 
-// Replaces a scratch block by one of `need` bytes.
-static int regrow(zha_tree *t, void **block, size_t *bytes, size_t need, const char *what) {
-    if (t->capturing)
-        return fail(ZHA_ERR_INVALID, "the captured call needs more scratch than the tree holds: make it once, or call "
-                                     "zha_reserve, before capturing");
-    if (*block && t->captured) {  // a graph may still use it
-        zha_retired *r = new (std::nothrow) zha_retired{*block, t->retired};
-        if (!r) return fail(ZHA_ERR_OOM, "host allocation failed");
-        t->retired = r;
-    } else if (*block) {
-        cudaFree(*block);
-    }
-    *block = nullptr;
-    *bytes = 0;
-    cudaError_t e = cudaMalloc(block, need);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
+// Makes a scratch block at least `need` bytes. in_graph: a captured call uses the block.
+static int grow(zha_tree *t, void **block, size_t *bytes, bool *in_graph, size_t need, bool captured, const char *what) {
+    if (need > *bytes) {
+        if (captured)
+            return fail(ZHA_ERR_INVALID, "the captured call needs more scratch than the tree holds: make it once before "
+                                         "capturing, or (search, attend) call zha_reserve");
+        if (*block && *in_graph) {
+            zha_retired *r = new (std::nothrow) zha_retired{*block, t->retired};
+            if (!r) return fail(ZHA_ERR_OOM, "host allocation failed");
+            t->retired = r;
+        } else if (*block) {
+            cudaFree(*block);
+        }
         *block = nullptr;
-        return cuda_fail(e, what);
+        *bytes = 0;
+        *in_graph = false;
+        cudaError_t e = cudaMalloc(block, need);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            *block = nullptr;
+            return cuda_fail(e, what);
+        }
+        *bytes = need;
     }
-    *bytes = need;
+    *in_graph |= captured;
     return ZHA_OK;
 }
 
 // Carves the scratch of one search/attend of `walks` walks out of one device
 // allocation (grown when too small).
-int reserve(zha_tree *t, long long walks, int max_sel, Scratch *s) {
+int reserve(zha_tree *t, long long walks, int max_sel, Scratch *s, bool captured) {
     const zha_config &c = t->cfg;
     const long long W = walks < 1 ? 1 : walks;
     (void)max_sel;  // the layout depends on the walks and the tree only
@@ -252,12 +258,8 @@ int reserve(zha_tree *t, long long walks, int max_sel, Scratch *s) {
         if (maxn_b > 0) tcl = tc_layout(t->T, Gw, maxn_b, maxn_sparse, c.R);
     }
     const size_t o_tc = take(tcl.bytes);
-    const size_t need = off;
-
-    if (need > t->ws_bytes) {
-        const int rc = regrow(t, &t->ws, &t->ws_bytes, need, "allocating search scratch");
-        if (rc) return rc;
-    }
+    const int rc = grow(t, &t->ws, &t->ws_bytes, &t->ws_in_graph, off, captured, "allocating search scratch");
+    if (rc) return rc;
     char *b = static_cast<char *>(t->ws);
     s->qf = reinterpret_cast<float *>(b + o_qf);
     s->S = reinterpret_cast<float *>(b + o_S);
@@ -509,9 +511,9 @@ int zha_search(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads, int
     } else {
         return fail(ZHA_ERR_INVALID, "mode must be ZHA_TOP_P or ZHA_TOP_K");
     }
-    zha::note_capture(t, static_cast<cudaStream_t>(stream));
+    const bool captured = zha::is_captured(static_cast<cudaStream_t>(stream));
     zha::Scratch s;
-    rc = zha::reserve(t, W, max_sel, &s);
+    rc = zha::reserve(t, W, max_sel, &s, captured);
     if (rc) return rc;
     ZHA_CUDA(zha::launch_search(t, s, Q, q_dtype, G, W, mode, p, k, sel, sel_count, max_sel, stats, start_level(t),
                                 static_cast<cudaStream_t>(stream)),
@@ -554,7 +556,7 @@ int zha_cp_begin(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads, i
             break;
         }
     zha::Scratch s;
-    rc = zha::reserve(t, W, 1, &s);
+    rc = zha::reserve(t, W, 1, &s, zha::is_captured(static_cast<cudaStream_t>(stream)));
     if (rc) return rc;
     ZHA_CUDA(zha::launch_search_init(t, s, Q, q_dtype, G, W, nullptr, s0, static_cast<cudaStream_t>(stream)),
              "launching the walk set-up");
@@ -574,9 +576,9 @@ int zha_cp_export(zha_tree *t, int *ids, float *scores, int *counts, long long l
     if (!t->cp_active) return fail(ZHA_ERR_INVALID, "no context-parallel walk is in progress (zha_cp_begin)");
     if (list_stride < 1) return fail(ZHA_ERR_INVALID, "list_stride must be >= 1");
     zha::Scratch s;
-    int rc = zha::reserve(t, t->cp_W, 1, &s);
-    if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int rc = zha::reserve(t, t->cp_W, 1, &s, zha::is_captured(st));
+    if (rc) return rc;
     const int l = t->cp_level;
     ZHA_CUDA(zha::launch_score_level(t, s, l, t->cp_G, st), "launching the shard's scoring");
     ZHA_CUDA(zha::launch_cp_export(t, s, t->cp_cur, l, l == t->cp_start, t->cp_off[l], t->cp_W, ids, scores, counts,
@@ -602,14 +604,15 @@ int zha_cp_select(zha_tree *t, int n_parts, const int *ids, const float *scores,
     }
     const long long W = t->cp_W, P = (long long)n_parts * list_stride;
     if (P > (1LL << 30)) return fail(ZHA_ERR_INVALID, "n_parts * list_stride too large");
+    const bool captured = zha::is_captured(static_cast<cudaStream_t>(stream));
     zha::Scratch s;
-    int rc = zha::reserve(t, W, 1, &s);
+    int rc = zha::reserve(t, W, 1, &s, captured);
     if (rc) return rc;
     // packed lists, chosen ids and the selector's staging, per walk P slots each
     const size_t o_ps = align_up(sizeof(int) * W * P), o_pc = o_ps + align_up(sizeof(float) * W * P);
     const size_t o_op = o_pc + align_up(sizeof(int) * W), o_oc = o_op + align_up(sizeof(int) * W * P);
     const size_t o_st = o_oc + align_up(sizeof(int) * W);
-    rc = zha::grow_dense_scratch(t, o_st + align_up(sizeof(uint32_t) * W * P));
+    rc = zha::grow_dense_scratch(t, o_st + align_up(sizeof(uint32_t) * W * P), captured);
     if (rc) return rc;
     char *b = static_cast<char *>(t->dws);
     zha::CpScratch cs{reinterpret_cast<int *>(b), reinterpret_cast<float *>(b + o_ps), reinterpret_cast<int *>(b + o_pc),
@@ -651,14 +654,14 @@ int zha_attend(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads, int
     if (!sel || !sel_count || !out) return fail(ZHA_ERR_INVALID, "sel, sel_count and out must not be NULL");
     if (out_dtype != ZHA_F32 && out_dtype != ZHA_BF16) return fail(ZHA_ERR_INVALID, "out_dtype must be ZHA_F32 or ZHA_BF16");
     if (max_sel < 1) return fail(ZHA_ERR_INVALID, "max_sel must be >= 1");
-    zha::note_capture(t, static_cast<cudaStream_t>(stream));
+    const bool captured = zha::is_captured(static_cast<cudaStream_t>(stream));
     zha::Scratch s;
-    rc = zha::reserve(t, W, max_sel, &s);
+    rc = zha::reserve(t, W, max_sel, &s, captured);
     if (rc) return rc;
     if (aligned16(Q) && zha::attend_tc_applicable(t, G, q_dtype)) {  // its queries are copied 16 bytes at a time
         // many bf16 walks per tree: tree-major attention on the tensor cores, its
         // scratch from the tree's second block
-        rc = zha::grow_dense_scratch(t, zha::attend_tc_scratch(t, G, W));
+        rc = zha::grow_dense_scratch(t, zha::attend_tc_scratch(t, G, W), captured);
         if (rc) return rc;
         ZHA_CUDA(zha::launch_attend_tc(t, G, W, Q, sel, sel_count, max_sel, out, out_dtype, lse, t->dws,
                                        static_cast<cudaStream_t>(stream)),
@@ -689,9 +692,8 @@ int zha_attend_draft(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_head
     if (!aligned16(k_draft) || !aligned16(v_draft)) return fail(ZHA_ERR_INVALID, "k_draft and v_draft must be 16-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const zha::Draft dr{k_draft, v_draft, mask, draft_dtype, n_draft};
-    zha::note_capture(t, st);
     zha::Scratch s;
-    rc = zha::reserve(t, W, max_sel, &s);
+    rc = zha::reserve(t, W, max_sel, &s, zha::is_captured(st));
     if (rc) return rc;
     ZHA_CUDA(zha::launch_attend(t, s, Q, q_dtype, G, W, sel, sel_count, max_sel, out, out_dtype, lse, &dr, st),
              "launching the attention of drafted tokens");
@@ -701,9 +703,8 @@ int zha_attend_draft(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_head
 }  // extern "C"
 
 // Grows the tree's full-scan scratch to at least `need` bytes.
-int zha::grow_dense_scratch(zha_tree *t, size_t need) {
-    if (need <= t->dws_bytes) return ZHA_OK;
-    return regrow(t, &t->dws, &t->dws_bytes, need, "allocating full-scan scratch");
+int zha::grow_dense_scratch(zha_tree *t, size_t need, bool captured) {
+    return grow(t, &t->dws, &t->dws_bytes, &t->dws_in_graph, need, captured, "allocating full-scan scratch");
 }
 
 extern "C" {
@@ -724,7 +725,8 @@ int zha_chunk_mass(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads,
     const size_t o_S = align_up(sizeof(float) * W * t->cfg.d);
     const size_t o_Sc = o_S + align_up(sizeof(float) * W * N);
     const size_t o_gk = o_Sc + align_up(sizeof(float) * W * nch);
-    rc = zha::grow_dense_scratch(t, o_gk + align_up(sizeof(uint32_t) * W * nch));
+    rc = zha::grow_dense_scratch(t, o_gk + align_up(sizeof(uint32_t) * W * nch),
+                                 zha::is_captured(static_cast<cudaStream_t>(stream)));
     if (rc) return rc;
     char *b = static_cast<char *>(t->dws);
     ZHA_CUDA(zha::launch_chunk_mass(t, Q, q_dtype, G, W, group, p, sel, count, max_sel, reinterpret_cast<float *>(b),
@@ -753,7 +755,7 @@ int zha_dense_scan(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads,
     const long long N = t->n > 0 ? t->n : 1;
     const size_t need = align_up(sizeof(float) * W * t->cfg.d) + align_up(sizeof(float) * W * N) +
                         align_up(sizeof(uint32_t) * W * N);
-    rc = zha::grow_dense_scratch(t, need);
+    rc = zha::grow_dense_scratch(t, need, zha::is_captured(static_cast<cudaStream_t>(stream)));
     if (rc) return rc;
     char *b = static_cast<char *>(t->dws);
     float *qf = reinterpret_cast<float *>(b);
@@ -769,9 +771,8 @@ int zha_dense_scan(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads,
 int zha_reserve(zha_tree *t, long long max_walks, int max_sel) {
     if (!t) return fail(ZHA_ERR_INVALID, "tree is NULL");
     if (max_walks < 1 || max_sel < 1) return fail(ZHA_ERR_INVALID, "max_walks and max_sel must be >= 1");
-    t->capturing = 0;
     zha::Scratch s;
-    return zha::reserve(t, max_walks, max_sel, &s);
+    return zha::reserve(t, max_walks, max_sel, &s, false);
 }
 
 int zha_level(const zha_tree *t, int level, const float **nodes, long long *n_nodes, long long *level_capacity,
@@ -847,9 +848,9 @@ int zha_last_search_info(zha_tree *t, zha_search_info *out, void *stream) {
     memset(out, 0, sizeof *out);
     if (t->last_W < 1) return fail(ZHA_ERR_INVALID, "no search has run on this tree");
     zha::Scratch s;
-    int rc = zha::reserve(t, t->last_W, t->last_max_sel, &s);
-    if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int rc = zha::reserve(t, t->last_W, t->last_max_sel, &s, zha::is_captured(st));
+    if (rc) return rc;
     unsigned long long *d = nullptr;
     ZHA_CUDA(cudaMalloc(&d, sizeof(unsigned long long) * 2 * (ZHA_MAX_DEPTH + 1)), "allocating counters");
     cudaMemsetAsync(d, 0, sizeof(unsigned long long) * 2 * (ZHA_MAX_DEPTH + 1), st);

@@ -255,9 +255,9 @@ struct zha_tree {
     void *dws;
     size_t dws_bytes;
 
-    // A CUDA graph that captured a call keeps the addresses of its scratch: from
-    // the first captured call on, a block that is outgrown is kept until zha_destroy.
-    int captured, capturing;
+    // A CUDA graph that captured a call keeps the addresses of its scratch: a block
+    // that a captured call used is kept until zha_destroy when it is outgrown.
+    bool ws_in_graph, dws_in_graph;
     struct zha_retired *retired;
 
     // diagnostics
@@ -300,9 +300,11 @@ struct Scratch {
     long long Sstride, Lstride, max_items, max_groups;
 };
 
-int reserve(zha_tree *t, long long walks, int max_sel, Scratch *s);
-// Notes whether `st` is being captured, for the scratch of the call that follows.
-void note_capture(zha_tree *t, cudaStream_t st);
+// Whether work sent to `st` goes into a graph.
+bool is_captured(cudaStream_t st);
+// The scratch of one search or attend of `walks` walks; `captured`: the call goes into a
+// graph (then nothing is allocated, and the block is kept as long as the tree).
+int reserve(zha_tree *t, long long walks, int max_sel, Scratch *s, bool captured);
 
 // Packed lists of a context-parallel level step (carved from the tree's second
 // scratch block): per walk P = n_parts * list stride slots.
@@ -351,8 +353,9 @@ cudaError_t launch_score_tc_sparse(const zha_tree *t, int level, int G, const vo
 // Records an error message for zha_last_error (this host thread); returns code.
 int set_error(int code, const char *msg);
 // Grows the tree's second scratch block (full-scan indexer, chunk-mass profile,
-// split-loss gradient) to at least `need` bytes; returns a ZHA_ status.
-int grow_dense_scratch(zha_tree *t, size_t need);
+// split-loss gradient) to at least `need` bytes (`captured` as for reserve); returns a
+// ZHA_ status.
+int grow_dense_scratch(zha_tree *t, size_t need, bool captured);
 
 // kernel launchers (return cudaError_t of the launch)
 cudaError_t launch_build_level(const zha_tree *t, int level, long long j0, long long j1,

@@ -371,7 +371,7 @@ extern "C" int zha_ref_grad(zha_tree *t, const void *Q, zha_dtype q_dtype, int n
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // the tree's second scratch block, shared with the full-scan indexer (grown
     // when too small, then reused by later calls)
-    const int rc = zha::grow_dense_scratch(t, o);
+    const int rc = zha::grow_dense_scratch(t, o, zha::is_captured(st));
     if (rc) return rc;
     char *b = static_cast<char *>(t->dws);
     cudaError_t e = cudaMemsetAsync(b + off[6], 0, gbytes, st);
