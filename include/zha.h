@@ -458,7 +458,13 @@ int zha_lse_combine(int n_parts, long long walks, int d, const float *outs, cons
 /*
  * zha_reserve: allocate the search and attend scratch for up to max_walks walks
  * and selections of up to max_sel chunks now, so that later calls with at most
- * these sizes allocate nothing (e.g. before capturing them in a CUDA graph).
+ * these sizes allocate nothing (e.g. before capturing them in a CUDA graph), for as
+ * many keys as the capacity. Where bf16 queries would bring that many walks to the
+ * tensor-core attention (d = 128, chunks of 8 to 64 keys, a power of two; from 1,024
+ * walks a tree over a bf16 cache and 4,096 over an 8-bit one), that is a copy of the
+ * capacity's values in bf16, over an 8-bit cache of its keys too, and 4 (walks a tree)
+ * (capacity / 128 + capacity / (32 chunk)) bytes a tree beside the rest.
+ * Errors: ZHA_ERR_INVALID, ZHA_ERR_OOM.
  * Every call that takes scratch: captured, it is refused (ZHA_ERR_INVALID, the
  * capture goes on) if it would have to allocate, whatever the capture's mode; and
  * scratch that it used is kept until zha_destroy when a larger call outgrows it, so

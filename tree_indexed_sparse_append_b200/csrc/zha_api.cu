@@ -189,7 +189,7 @@ static int grow(zha_tree *t, void **block, size_t *bytes, bool *in_graph, size_t
     if (need > *bytes) {
         if (captured)
             return fail(ZHA_ERR_INVALID, "the captured call needs more scratch than the tree holds: make it once before "
-                                         "capturing, or (search, attend) call zha_reserve");
+                                         "capturing, or (search, attention) call zha_reserve");
         if (*block && *in_graph) {
             zha_retired *r = new (std::nothrow) zha_retired{*block, t->retired};
             if (!r) return fail(ZHA_ERR_OOM, "host allocation failed");
@@ -661,7 +661,7 @@ int zha_attend(zha_tree *t, const void *Q, zha_dtype q_dtype, int n_q_heads, int
     if (aligned16(Q) && zha::attend_tc_applicable(t, G, q_dtype)) {  // its queries are copied 16 bytes at a time
         // many bf16 walks per tree: tree-major attention on the tensor cores, its
         // scratch from the tree's second block
-        rc = zha::grow_dense_scratch(t, zha::attend_tc_scratch(t, G, W), captured);
+        rc = zha::grow_dense_scratch(t, zha::attend_tc_scratch(t, G, t->n, t->n_nodes[1]), captured);
         if (rc) return rc;
         ZHA_CUDA(zha::launch_attend_tc(t, G, W, Q, sel, sel_count, max_sel, out, out_dtype, lse, t->dws,
                                        static_cast<cudaStream_t>(stream)),
@@ -772,7 +772,11 @@ int zha_reserve(zha_tree *t, long long max_walks, int max_sel) {
     if (!t) return fail(ZHA_ERR_INVALID, "tree is NULL");
     if (max_walks < 1 || max_sel < 1) return fail(ZHA_ERR_INVALID, "max_walks and max_sel must be >= 1");
     zha::Scratch s;
-    return zha::reserve(t, max_walks, max_sel, &s, false);
+    const int rc = zha::reserve(t, max_walks, max_sel, &s, false);
+    if (rc) return rc;
+    // the attention of many bf16 walks takes the second block, for the keys the tree may come to hold
+    const int G = zha::attend_tc_walks(t, max_walks / t->T);
+    return G ? zha::grow_dense_scratch(t, zha::attend_tc_scratch(t, G, t->cfg.capacity, t->cap_nodes[1]), false) : ZHA_OK;
 }
 
 int zha_level(const zha_tree *t, int level, const float **nodes, long long *n_nodes, long long *level_capacity,

@@ -484,20 +484,25 @@ __global__ void atc_finish_kernel(const unsigned *mkey, const float *lsum, const
 
 }  // namespace
 
-bool attend_tc_applicable(const zha_tree *t, int G, zha_dtype q_dtype) {
+int attend_tc_walks(const zha_tree *t, long long G) {
     const zha_config &c = t->cfg;
     // chunks of 8 to 64 keys (powers of two): a tile's chunk mask fits in 16 bits. An 8-bit
     // cache's blocks of walks take less time up to some 3,700 walks a tree (256K keys,
     // 1,300 keys a walk: 1,008 walks 0.45 ms there and 1,024 here 1.51 ms; here 4,096 walks
     // 1.64 ms, four times 1,008 there 1.8)
-    if (c.kv_dtype == ZHA_E4M3 && G < TC_E4M3_MIN_G) return false;
-    return c.d == TC_K && c.kv_dtype != ZHA_F32 && q_dtype == ZHA_BF16 && G >= TC_MIN_G && G <= 65535 &&
-           c.chunk >= 8 && c.chunk <= 64 && (c.chunk & (c.chunk - 1)) == 0 && t->n > 0;
+    const int least = c.kv_dtype == ZHA_E4M3 ? TC_E4M3_MIN_G : TC_MIN_G;
+    if (c.d != TC_K || c.kv_dtype == ZHA_F32 || G < least || c.chunk < 8 || c.chunk > 64 || (c.chunk & (c.chunk - 1)))
+        return 0;
+    return G < 65535 ? (int)G : 65535;
 }
 
-size_t attend_tc_scratch(const zha_tree *t, int G, long long W) {
-    const long long ntiles = (t->n + AT_KEYS - 1) / AT_KEYS;
-    const long long words1 = t->n_nodes[1] > 0 ? (t->n_nodes[1] + 31) / 32 : 1;
+bool attend_tc_applicable(const zha_tree *t, int G, zha_dtype q_dtype) {
+    return q_dtype == ZHA_BF16 && t->n > 0 && attend_tc_walks(t, G) == G;
+}
+
+size_t attend_tc_scratch(const zha_tree *t, int G, long long n, long long n1) {
+    const long long ntiles = (n + AT_KEYS - 1) / AT_KEYS, W = (long long)t->T * G;
+    const long long words1 = n1 > 0 ? (n1 + 31) / 32 : 1;
     auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
     return al(sizeof(unsigned) * t->T * words1 * G) + al(sizeof(int) * t->T * ntiles) +
            al(sizeof(unsigned) * t->T * ntiles * G) + al((size_t)t->T * ntiles * TC_PART) + al(sizeof(unsigned) * W) +

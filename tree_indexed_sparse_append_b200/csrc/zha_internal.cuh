@@ -398,7 +398,10 @@ cudaError_t launch_lse_combine(int n_parts, long long W, int D, const float *out
 // Final attention on the tensor cores for trees walked by many bf16 queries
 // (zha_attend_tc.cu): applicability, scratch bytes, and the launch (scratch at ws).
 bool attend_tc_applicable(const zha_tree *t, int G, zha_dtype q_dtype);
-size_t attend_tc_scratch(const zha_tree *t, int G, long long W);
+// The most walks a tree, up to G, that bf16 queries bring to it (0: none).
+int attend_tc_walks(const zha_tree *t, long long G);
+// for G walks over n keys and n1 level-1 nodes a tree
+size_t attend_tc_scratch(const zha_tree *t, int G, long long n, long long n1);
 cudaError_t launch_attend_tc(const zha_tree *t, int G, long long W, const void *Q, const int *sel,
                              const int *sel_count, int max_sel, void *out, zha_dtype out_dtype, float *lse,
                              void *ws, cudaStream_t st);
