@@ -278,8 +278,11 @@ int zha_search(zha_tree *tree, const void *Q, zha_dtype q_dtype, int n_q_heads, 
  * The ids of a walk are distinct, as zha_search writes them (over an 8-bit cache, and
  * in zha_attend_draft, an id given twice counts once).
  * Over an 8-bit cache walks of one tree are taken 8 or 16 at a time, and a row that
- * several of them chose is read once; queries and weights are rounded to at least
- * 22 bits for an fp32 out and to 11 bits for a bf16 one, sums are fp32, and a call
+ * several of them chose is read once. Queries and weights are rounded to at least
+ * 22 bits for an fp32 out and to 11 bits for a bf16 one; a weight that is small beside
+ * the walk's others may lose more of itself, but no key adds more than 2^-22 (2^-18
+ * for a bf16 out) of max_c sum_i p_i |v_ic| to the result's error that way, whatever
+ * the sizes of the values that this walk and others chose. Sums are fp32, and a call
  * gives the same bits each time (from 4,096 bf16 walks a tree on at d = 128, where
  * the tensor-core kernels of a bf16 cache take it, the same values to fp32
  * rounding). A NaN reaches only the walks that attend to it (with those kernels, every

@@ -45,7 +45,7 @@
 // A value that is not finite reaches every walk of the block through a weight of
 // zero (0 * NaN). So a walk with a NaN among its sums is computed again by itself,
 // over its own keys (slow_walk): only those that attend to a NaN give NaN. So is a walk
-// all of whose values are far below the block's (VFAR_ONE).
+// whose sums are small beside the block's largest values (VSUM_ONE).
 //
 // Measured, 8-bit cache, d = 128, bf16, 4 heads a KV head: 256 walks of 96 chunks of 8
 // over 262,144 keys 19.4 us a call (the item kernel, a walk at a time: 39), 1,024 walks of
@@ -73,12 +73,16 @@ constexpr int WINDOW = 1024;       // chunks whose ids and masks are held at a t
 constexpr float NEAR = 5.5f;
 constexpr int PSHIFT = 7;
 constexpr float LOG2E = 1.4426950408889634f;
-// An 8-bit cache's weights are scaled by their values' powers of two over the largest
-// that the warp has met, any walk's, before they are rounded; fp16 ends at 2^-24. A walk
-// whose own values are all more than 2^VFAR below that has lost too much of them (2^-25 of
-// the largest weight is kept of two terms, 2^-20 of one) and is computed by itself.
+// An 8-bit cache's weights are scaled by 2^(PSHIFT + e - vref) before they are rounded: e the
+// value's power of two, vref the largest that the warp has met, any walk's. fp16 ends at 2^-24,
+// so a small one is rounded to a multiple of that, and not to its own 11 bits (22 of two terms).
+// Where no value of a part is more than 2^VFAR below the largest, that is an error of at most
+// 2^-20 (2^-24) of the walk's heaviest weight, which is 1 or more. Where some are, what a walk
+// has lost shows in its sums: a code is at most 448, so a key adds an error of at most 448 * 2^-25
+// to a sum, 2^-18 (2^-22) of the walk's largest if that is 2^VSUM or more. A walk whose sums are
+// all smaller is computed by itself.
 constexpr int VFAR_ONE = 12, VFAR_TWO = 8;
-constexpr unsigned BYTE_ZERO = 10;  // the exponent byte of a row of zeros
+constexpr int VSUM_ONE = 2, VSUM_TWO = 6;
 
 // NW: groups of 8 walks a block. FAST: bf16 queries and results (an 8-bit or bf16 cache):
 // one term of the query, one (8-bit) or two of a weight, summed in the accumulators. DRAFT:
@@ -501,8 +505,8 @@ __device__ __forceinline__ const unsigned char *mask_row(const BlockArgs &a, con
     return a.mask + ((long long)(p.tree / a.H_kv) * nd + (int)((p.walk0 + w) % nd)) * nd;
 }
 
-// One walk over the part's keys that it chose, by a warp on the CUDA cores: the way of
-// a walk whose sums hold a NaN, which may be another walk's.
+// One walk over the part's keys that it chose, by a warp on the CUDA cores with fp32 weights:
+// the way of a walk whose sums hold a NaN, which may be another walk's, or have lost too much.
 template <typename KT, int D, typename S>
 __device__ __noinline__ void slow_walk(const BlockArgs &a, const Part &p, const S &s, int w, int cnt, bool drafted,
                                        float &m, float &l, float (&o)[D / 32]) {
@@ -558,27 +562,6 @@ __device__ __noinline__ void slow_walk(const BlockArgs &a, const Part &p, const 
         load_cols<N>(a.vd, a.d_bf16, ((long long)p.tree * a.n_draft + j) * D + lane * N, vx);
         add(kx, vx);
     }
-}
-
-// Whether walk w has values in the part, none zero or as large as exponent byte `from`. A warp.
-template <typename S>
-__device__ __noinline__ bool values_below(const BlockArgs &a, const Part &p, const S &s, int w, int cnt, unsigned from) {
-    const int lane = threadIdx.x & 31;
-    const unsigned char *Vs = a.Vs + p.tree * a.cap;
-    const int *list = a.sel + (p.walk0 + w) * a.max_sel;
-    unsigned top = 0u;
-    for (int i = 0; i < cnt; i += 32) {
-        const int c = i + lane < cnt ? __ldg(list + i + lane) : -1;
-        if (c >= 0 && c < a.n1) {
-            const int kp = rank_of(s.bits, s.pre, c) * a.C;
-            for (int j = max(0, p.k0 - kp); j < min(a.C, p.k1 - kp); ++j) top = max(top, (unsigned)__ldg(Vs + (long long)c * a.C + j));
-        }
-        if (__any_sync(FULL, top >= from)) return false;
-    }
-    for (int kp = max(p.k0, p.U * a.C) + lane; kp < p.k1; kp += 32)
-        top = max(top, (unsigned)__ldg(Vs + (long long)a.n1 * a.C + (kp - p.U * a.C)));
-    top = __reduce_max_sync(FULL, top);
-    return top > BYTE_ZERO && top < from;
 }
 
 template <typename KT, int D, int NW, bool FAST, bool DRAFT>
@@ -785,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NW, FAST, DRAFT>::WARPS * 32, Cfg<K
             rs[n][c] = a.beta / s_up[n * 8 + 2 * t4 + c];
         }
     int vref = 1;  // exponent byte that the sums of values are scaled by
-    int vlow = 255;  // the least of this lane's rows that are not zero
+    int vlow = 255;  // the least of this lane's rows
 
     // Online softmax of a tile: sc (keys g, g + 8) becomes the weights, scaled
     // as V is. walks: of the two keys, shifted down by 2 t4; kf: their powers of two; ve:
@@ -896,7 +879,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NW, FAST, DRAFT>::WARPS * 32, Cfg<K
             if (lane < 16) s_meta[warp][i % STAGES][lane] = make_uint2(k.walks, (k.ke << 23) | k.ve);
             if constexpr (F8) {
                 vtop = __reduce_max_sync(FULL, (int)k.ve);
-                vlow = min(vlow, k.ve > BYTE_ZERO ? (int)k.ve : 255);
+                vlow = min(vlow, k.walks ? (int)k.ve : 255);
             }
         };
         const Key first = fetch(0);
@@ -1292,7 +1275,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NW, FAST, DRAFT>::WARPS * 32, Cfg<K
                 for (int j = 0; j < MT; ++j) sum[w * C::MS + j * 16 + (c >> 1) * 8 + g] = acc[j][n][c] * down * back;
             }
         __syncthreads();
-        int vfar = 0;  // exponent byte below which values are far from the largest (0: none is)
+        float vsum = 0.f;  // sums below this have lost too much to the largest values
         if constexpr (F8) {
             int vmax = 0, vmin = 255;
 #pragma unroll
@@ -1300,8 +1283,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NW, FAST, DRAFT>::WARPS * 32, Cfg<K
                 vmax = max(vmax, s_vmax[x]);
                 vmin = min(vmin, s_vmin[x]);
             }
-            const int from = vmax - (FAST || p_terms == 1 ? VFAR_ONE : VFAR_TWO);
-            if (vmin < from) vfar = from;
+            const bool one = FAST || p_terms == 1;
+            if (vmin < vmax - (one ? VFAR_ONE : VFAR_TWO))
+                vsum = exp_byte((unsigned)vmax) * exp_byte((unsigned)(127 - PSHIFT + (one ? VSUM_ONE : VSUM_TWO)));
         }
         for (int w = warp; w < p.nw; w += WARPS) {
             float mm = -INFINITY, ll = 0.f, o[N];
@@ -1322,25 +1306,25 @@ __global__ void __launch_bounds__(Cfg<KT, D, NW, FAST, DRAFT>::WARPS * 32, Cfg<K
                 }
             }
             bool bad = false;
+            float top = 0.f;
 #pragma unroll
-            for (int c = 0; c < N; ++c) bad |= o[c] != o[c];
+            for (int c = 0; c < N; ++c) {
+                bad |= o[c] != o[c];
+                top = fmaxf(top, fabsf(o[c]));
+            }
+            if (F8 && vsum > 0.f) bad |= ll > 0.f && warp_max(top) < vsum;
             bad = __any_sync(FULL, bad);
-            if ((F8 && vfar) || bad) {
+            if (bad) {
                 // copies: what is passed by its address lies in local memory, in the tiles' loop too (1.1 to
                 // 1.25 times the call's time)
                 const Part pp = p;
                 const Smem<C> ss(smem_blocks, a);
                 float m2, l2, o2[N];
-                if constexpr (F8) {
-                    if (!bad) bad = values_below(a, pp, ss, w, s_cnt[w], (unsigned)vfar);
-                }
-                if (bad) {
-                    slow_walk<KT, D>(a, pp, ss, w, s_cnt[w], drafted, m2, l2, o2);
-                    mm = m2;
-                    ll = l2;
+                slow_walk<KT, D>(a, pp, ss, w, s_cnt[w], drafted, m2, l2, o2);
+                mm = m2;
+                ll = l2;
 #pragma unroll
-                    for (int c = 0; c < N; ++c) o[c] = o2[c];
-                }
+                for (int c = 0; c < N; ++c) o[c] = o2[c];
             }
             if (np == 1) {
                 finish_walk<D>(a, p.walk0 + w, lane, mm, ll, o);
