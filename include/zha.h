@@ -275,8 +275,8 @@ int zha_search(zha_tree *tree, const void *Q, zha_dtype q_dtype, int n_q_heads, 
  * out: [B][H_q][n_q][d] of out_dtype (the fp32 result, rounded to nearest even
  *      for ZHA_BF16); lse: [walks] fp32 (may be NULL).
  * A walk with no key at all (n == 0) gets out = 0 and lse = -inf.
- * The ids of a walk are distinct, as zha_search writes them (over an 8-bit cache, and
- * in zha_attend_draft, an id given twice counts once).
+ * The ids of a walk must be distinct, as zha_search writes them: an id given twice may
+ * count once or twice, here and in zha_attend_draft and zha_attend_noalloc.
  * Over an 8-bit cache walks of one tree are taken 8 or 16 at a time, and a row that
  * several of them chose is read once. Queries and weights are rounded to at least
  * 22 bits for an fp32 out and to 11 bits for a bf16 one; a weight that is small beside

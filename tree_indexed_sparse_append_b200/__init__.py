@@ -360,8 +360,9 @@ class Tree:
 
     def attend(self, Q: torch.Tensor, sel: torch.Tensor, sel_count: torch.Tensor, out=None, lse=None,
                out_dtype=None, stream=None):
-        """Returns (out [B][H_q][n_q][d] of out_dtype (default: the cache dtype; of an
-        E4M3 cache, Q's), lse [walks] fp32)."""
+        """Attention of each walk over its chosen chunks (distinct ids, in any order) and
+        the tail. Returns (out [B][H_q][n_q][d] of out_dtype (default: the cache dtype; of
+        an E4M3 cache, Q's), lse [walks] fp32)."""
         B, Hq, nq, d = Q.shape
         W = B * Hq * nq
         if out is None:
