@@ -1346,13 +1346,12 @@ template <typename KT, int D, int NW, bool FAST, bool DRAFT>
 cudaError_t launch_blocks(const zha_tree *t, BlockArgs a, cudaStream_t st) {
     using C = Cfg<KT, D, NW, FAST, DRAFT>;
     const size_t smem = C::FIXED + C::DTERMS * C::QBYTES + 8 * (size_t)a.words;
-    static thread_local int set_on = -1;  // the attribute is per device
-    if (set_on != t->device) {
-        cudaError_t e = cudaFuncSetAttribute(attend_block_kernel<KT, D, NW, FAST, DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::FIXED + C::DTERMS * C::QBYTES + (int)(BLOCK_CHUNKS_MAX / 32) * 8);
-        if (e != cudaSuccess) return e;
-        set_on = t->device;
-    }
+    static OncePerDevice limit;
+    cudaError_t e = limit(t->device, [] {
+        return cudaFuncSetAttribute(attend_block_kernel<KT, D, NW, FAST, DRAFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::FIXED + C::DTERMS * C::QBYTES + (int)(BLOCK_CHUNKS_MAX / 32) * 8);
+    });
+    if (e != cudaSuccess) return e;
     if (a.target) {
         // Few blocks: as many items as CTAs fit on the GPU, less one a block for the
         // rounding of each block's keys. More blocks: long ones are cut so that the last
@@ -1361,7 +1360,7 @@ cudaError_t launch_blocks(const zha_tree *t, BlockArgs a, cudaStream_t st) {
         const bool few = a.NB <= slots / 2;
         a.target = few ? slots - a.NB : 2 * slots;
         a.many = !few;
-        const cudaError_t e = launch_plan(t, a, st);
+        e = launch_plan(t, a, st);
         if (e != cudaSuccess) return e;
     }
     Probe pr(t, ZHA_K_ATTEND_PARTIAL, st);

@@ -558,15 +558,13 @@ cudaError_t launch_attend_tc(const zha_tree *t, int G, long long W, const void *
         a.kcap = a.ntiles * AT_KEYS;
     }
 
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(atc_max_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_MAX);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(atc_accum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ACC);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
-    cudaError_t e;
+    static OncePerDevice smem;
+    cudaError_t e = smem(t->device, [] {
+        const cudaError_t m = cudaFuncSetAttribute(atc_max_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_MAX);
+        return m != cudaSuccess ? m
+                                : cudaFuncSetAttribute(atc_accum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ACC);
+    });
+    if (e != cudaSuccess) return e;
     const dim3 tiles((unsigned)a.ntiles, (unsigned)t->T);
     {
         Probe pr(t, ZHA_K_ATTEND_PLAN, st);

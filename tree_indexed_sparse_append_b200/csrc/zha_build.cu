@@ -703,13 +703,11 @@ template <typename CT, int D>
 cudaError_t launch_build_typed(const zha_tree *t, const BuildArgs &a, cudaStream_t st) {
     const int threads = 32 * a.R;
     const size_t smem = (size_t)a.R * (a.C * 33 + a.C) * sizeof(float);
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(build_nodes_kernel<CT, D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static OncePerDevice limit;
+    const cudaError_t e = limit(t->device, [] {
+        return cudaFuncSetAttribute(build_nodes_kernel<CT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    });
+    if (e != cudaSuccess) return e;
     long long blocks = a.items;
     const long long cap = (long long)num_sms() * 16;
     if (blocks > cap) blocks = cap;

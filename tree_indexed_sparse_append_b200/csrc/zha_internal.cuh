@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "../../include/zha.h"
+#include "zha_once.cuh"
 
 namespace zha {
 

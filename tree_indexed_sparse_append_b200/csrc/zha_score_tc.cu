@@ -673,13 +673,11 @@ __global__ void __launch_bounds__(128, 1) score_tc_sparse_kernel(SparseArgs a) {
 
 template <int RP>
 cudaError_t launch_sparse_rp(const zha_tree *t, const SparseArgs &sa, cudaStream_t st) {
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e =
-            cudaFuncSetAttribute(score_tc_sparse_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, TS_SMEM);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static OncePerDevice smem;
+    const cudaError_t e = smem(t->device, [] {
+        return cudaFuncSetAttribute(score_tc_sparse_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, TS_SMEM);
+    });
+    if (e != cudaSuccess) return e;
     Probe pr(t, ZHA_K_SCORE_TC, st);
     long long grid = sa.ntiles * t->T;  // persistent: one CTA per SM at most
     if (grid > num_sms()) grid = num_sms();
@@ -765,13 +763,11 @@ bool tc_sparse_applicable(const zha_tree *t, int G, const void *Q, zha_dtype q_d
 namespace {
 template <int RP>
 cudaError_t launch_score_tc_rp(const zha_tree *t, const ScoreTcArgs &sa, cudaStream_t st) {
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e =
-            cudaFuncSetAttribute(score_tc_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static OncePerDevice smem;
+    const cudaError_t e = smem(t->device, [] {
+        return cudaFuncSetAttribute(score_tc_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM);
+    });
+    if (e != cudaSuccess) return e;
     Probe pr(t, ZHA_K_SCORE_TC, st);
     score_tc_kernel<RP><<<dim3((unsigned)(sa.mtiles / TC_MT), (unsigned)t->T), TC_THREADS, TC_SMEM, st>>>(sa);
     return cudaGetLastError();

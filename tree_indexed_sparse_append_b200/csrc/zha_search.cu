@@ -1103,14 +1103,13 @@ cudaError_t launch_select_warp(const SelectArgs &se, long long W, cudaStream_t s
 }
 
 template <int NT, int KB = 1>
-cudaError_t launch_select(const SelectArgs &se, long long W, cudaStream_t st) {
-    static bool smem_set = false;
-    if (!smem_set) {
-        cudaError_t e = cudaFuncSetAttribute(select_level_kernel<NT, KB>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * (int)sizeof(uint32_t));
-        if (e != cudaSuccess) return e;
-        smem_set = true;
-    }
+cudaError_t launch_select(const zha_tree *t, const SelectArgs &se, long long W, cudaStream_t st) {
+    static OncePerDevice smem;
+    const cudaError_t e = smem(t->device, [] {
+        return cudaFuncSetAttribute(select_level_kernel<NT, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    16384 * (int)sizeof(uint32_t));
+    });
+    if (e != cudaSuccess) return e;
     return launch_chained(select_level_kernel<NT, KB>, dim3((unsigned)W), dim3(NT),
                           (size_t)se.smem_keys * sizeof(uint32_t), st, se);
 }
@@ -1190,10 +1189,10 @@ cudaError_t launch_select_all(const zha_tree *t, const float *S, uint32_t *gkey,
     Probe pr(t, ZHA_K_SELECT, st);
     if (N > 8192) {
         se.smem_keys = std::min<long long>(N, 16384);
-        return N > 16384 ? launch_select<1024, 8>(se, W, st) : launch_select<1024>(se, W, st);
+        return N > 16384 ? launch_select<1024, 8>(t, se, W, st) : launch_select<1024>(t, se, W, st);
     }
     se.smem_keys = N;
-    return launch_select<256>(se, W, st);
+    return launch_select<256>(t, se, W, st);
 }
 
 cudaError_t launch_search_init(const zha_tree *t, const Scratch &s, const void *Q, zha_dtype q_dtype, int G,
@@ -1332,19 +1331,19 @@ cudaError_t launch_search(const zha_tree *t, const Scratch &s, const void *Q, zh
                 // walks' CTAs share an SM (measured on B200: 7.31 -> 6.68 ms for the
                 // prefill workload's search)
                 se.smem_keys = 4096;
-                e = launch_select<256>(se, W, st);
+                e = launch_select<256>(t, se, W, st);
             } else if (fmax > 8192) {
                 // few walks: the widest frontier sets the time, give it 1,024 threads
                 se.smem_keys = std::min<long long>(fmax, 16384);
-                e = launch_select<1024>(se, W, st);
+                e = launch_select<1024>(t, se, W, st);
             } else if (fmax > 2048 && W <= 2LL * num_sms()) {
                 // few walks over a level of thousands of nodes: frontiers of a few
                 // thousand keys, 512 threads
                 se.smem_keys = fmax;
-                e = launch_select<512>(se, W, st);
+                e = launch_select<512>(t, se, W, st);
             } else {
                 se.smem_keys = fmax;
-                e = launch_select<256>(se, W, st);
+                e = launch_select<256>(t, se, W, st);
             }
             if (e != cudaSuccess) return e;
         }
@@ -1585,13 +1584,13 @@ cudaError_t launch_cp_select(const zha_tree *t, const Scratch &s, int cur, int l
         Probe pr(t, ZHA_K_SELECT, st);
         if (P > 8192) {
             se.smem_keys = std::min<long long>(P, 16384);
-            e = launch_select<1024>(se, W, st);
+            e = launch_select<1024>(t, se, W, st);
         } else if (P > 2048) {
             se.smem_keys = P;
-            e = launch_select<512>(se, W, st);
+            e = launch_select<512>(t, se, W, st);
         } else {
             se.smem_keys = P;
-            e = launch_select<256>(se, W, st);
+            e = launch_select<256>(t, se, W, st);
         }
         if (e != cudaSuccess) return e;
     }
