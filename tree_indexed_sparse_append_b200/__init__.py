@@ -136,7 +136,7 @@ def _cache_code(t: torch.Tensor) -> int:
     return E4M3 if t.dtype == torch.float8_e4m3fn else _dtype_code(t)
 
 
-_SCALE_DTYPES = (torch.uint8, torch.float8_e8m0fnu)
+_SCALE_DTYPES = (torch.uint8, getattr(torch, "float8_e8m0fnu", torch.uint8))
 
 
 def _scale(t, K: torch.Tensor, dev: int, name: str) -> int:
@@ -201,8 +201,11 @@ def _dev(t: torch.Tensor, name: str) -> int:
 
 
 # the current stream's handle and the current device, without the objects around
-# them (torch.cuda.current_stream() takes 3 us)
-_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# them (torch.cuda.current_stream() takes 3 us) where torch has these names: one
+# built without CUDA lacks them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 
 def _stream(stream) -> int:
