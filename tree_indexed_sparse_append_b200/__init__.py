@@ -180,8 +180,8 @@ def _rows(t: torch.Tensor, name: str, dev: int):
 
 
 def _launch(f, dev: int, stream, *args) -> None:
-    """Calls f(*args, stream) with the tensors' device current, on its current stream
-    unless one is given."""
+    """Calls f(*args, stream) with the tensors' device current (a tree's own, whichever was),
+    on its current stream unless one is given."""
     s = stream.cuda_stream if stream is not None else _raw_stream(dev)
     if _get_device() == dev:
         rc = f(*args, s)
@@ -192,24 +192,12 @@ def _launch(f, dev: int, stream, *args) -> None:
         _check(rc)
 
 
-def _dev(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
 # the current stream's handle and the current device, without the objects around
 # them (torch.cuda.current_stream() takes 3 us) where torch has these names: one
 # built without CUDA lacks them
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
-
-
-def _stream(stream) -> int:
-    return stream.cuda_stream if stream is not None else _raw_stream(_get_device())
 
 
 class _DeviceArray:
@@ -244,16 +232,16 @@ class Tree:
         self.K, self.V, self.refs = K, V, refs
         self.k_scale, self.v_scale = k_scale, v_scale
         self._h = ctypes.c_void_p()
+        self._device = dev = _cuda_index(K, "K")
         if self.cfg.kv_dtype == E4M3:
-            dev = _cuda_index(K, "K")
-            _launch(lambda *a: lib().zha_build_scaled(*a, ctypes.byref(self._h)), dev, stream,
-                    ctypes.byref(self.cfg), _dev(K, "K"), _dev_of(V, "V", dev), _scale(k_scale, K, dev, "k_scale"),
-                    _scale(v_scale, K, dev, "v_scale"), _dev_of(refs, "refs", dev), int(n_keys))
-            return
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale and v_scale belong to an E4M3 cache")
-        _check(lib().zha_build(ctypes.byref(self.cfg), _dev(K, "K"), _dev(V, "V"), _dev(refs, "refs"),
-                               int(n_keys), _stream(stream), ctypes.byref(self._h)))
+            build = lib().zha_build_scaled
+            scales = _scale(k_scale, K, dev, "k_scale"), _scale(v_scale, K, dev, "v_scale")
+        else:
+            build, scales = lib().zha_build, ()
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("k_scale and v_scale belong to an E4M3 cache")
+        _launch(lambda *a: build(*a, ctypes.byref(self._h)), dev, stream, ctypes.byref(self.cfg), _dev_of(K, "K", dev),
+                _dev_of(V, "V", dev), *scales, _dev_of(refs, "refs", dev), int(n_keys))
 
     # -- properties -------------------------------------------------------
     @property
@@ -302,7 +290,8 @@ class Tree:
             return self.extend(k_new.unsqueeze(2), v_new.unsqueeze(2), stream=stream)
         if k_new.shape != (B, H, d) or v_new.shape != (B, H, d) or k_new.dtype != self.K.dtype or v_new.dtype != self.K.dtype:
             raise ValueError("k_new and v_new must be [B][H_kv][d] of the cache dtype")
-        _check(lib().zha_append(self._h, _dev(k_new, "k_new"), _dev(v_new, "v_new"), _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_append, dev, stream, self._h, _dev_of(k_new, "k_new", dev), _dev_of(v_new, "v_new", dev))
 
     def extend(self, k_new: torch.Tensor, v_new: torch.Tensor, rows: torch.Tensor | None = None,
                stream=None) -> None:
@@ -317,7 +306,7 @@ class Tree:
         if v_new.dtype != k_new.dtype or (self.cfg.kv_dtype != E4M3 and k_new.dtype != self.K.dtype):
             raise ValueError("k_new and v_new must be of one dtype, the cache's unless it is E4M3")
         src_rows = m = k_new.shape[2]
-        dev = self.K.get_device()
+        dev = self._device
         if rows is not None:
             if rows.dtype != torch.int32 or rows.dim() != 2 or rows.shape[0] != B:
                 raise ValueError("rows must be int32 [B][m]")
@@ -340,7 +329,7 @@ class Tree:
     def rebuild(self, stream=None) -> None:
         """Summarize every level again in place from the cache and the current
         refs (after the refs were updated in place); allocates nothing."""
-        _check(lib().zha_rebuild(self._h, _stream(stream)))
+        _launch(lib().zha_rebuild, self._device, stream, self._h)
 
     def search(self, Q: torch.Tensor, mode: int = TOP_P, p: float = 0.9, k: int = 1, max_sel: int | None = None,
                with_stats: bool = False, out=None, stream=None):
@@ -356,9 +345,10 @@ class Tree:
             st = torch.empty(W, STATS_BYTES, dtype=torch.uint8, device=Q.device) if with_stats else None
         else:
             sel, cnt, st = out
-        _check(lib().zha_search(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, mode, float(p), int(k),
-                                _dev(sel, "sel"), _dev(cnt, "sel_count"), max_sel,
-                                _dev(st, "stats") if st is not None else None, _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_search, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq, mode, float(p),
+                int(k), _dev_of(sel, "sel", dev), _dev_of(cnt, "sel_count", dev), max_sel,
+                _dev_of(st, "stats", dev) if st is not None else None)
         return sel, cnt, st
 
     def attend(self, Q: torch.Tensor, sel: torch.Tensor, sel_count: torch.Tensor, out=None, lse=None,
@@ -372,9 +362,10 @@ class Tree:
             out = torch.empty_like(Q, dtype=out_dtype or self._out_dtype(Q), memory_format=torch.contiguous_format)
         if lse is None:
             lse = Q.new_empty(W, dtype=torch.float32)
-        _check(lib().zha_attend(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, _dev(sel, "sel"),
-                                _dev(sel_count, "sel_count"), sel.shape[1], _dev(out, "out"), _dtype_code(out),
-                                _dev(lse, "lse"), _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_attend, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq,
+                _dev_of(sel, "sel", dev), _dev_of(sel_count, "sel_count", dev), sel.shape[1], _dev_of(out, "out", dev),
+                _dtype_code(out), _dev_of(lse, "lse", dev))
         return out, lse
 
     def _out_dtype(self, Q: torch.Tensor):
@@ -387,7 +378,7 @@ class Tree:
         that its row of mask [B][n][n] (bool or uint8) names. k_draft, v_draft
         [B][H_kv][n][d], fp32 or bf16. Returns (out, lse) as attend()."""
         B, H, _, d = self.K.shape
-        dev = self.K.get_device()
+        dev = self._device
         if Q.dim() != 4 or Q.shape[0] != B or Q.shape[3] != d or Q.shape[1] % H:
             raise ValueError("Q must be [B][H_q][n][d], H_q a multiple of H_kv")
         Hq, n = Q.shape[1], Q.shape[2]
@@ -420,10 +411,10 @@ class Tree:
         zha_attend_noalloc uses a fixed static device array as scratch. The caller
         provides out (and lse) already allocated; nothing is allocated here."""
         B, Hq, nq, d = Q.shape
-        _check(lib().zha_attend_noalloc(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, _dev(sel, "sel"),
-                                        _dev(sel_count, "sel_count"), sel.shape[1], _dev(out, "out"),
-                                        _dtype_code(out), _dev(lse, "lse") if lse is not None else None,
-                                        _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_attend_noalloc, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq,
+                _dev_of(sel, "sel", dev), _dev_of(sel_count, "sel_count", dev), sel.shape[1], _dev_of(out, "out", dev),
+                _dtype_code(out), _dev_of(lse, "lse", dev) if lse is not None else None)
         return out, lse
 
     def dense_scan(self, Q: torch.Tensor, mode: int = TOP_P, p: float = 0.9, k: int = 1,
@@ -439,8 +430,9 @@ class Tree:
             cnt = torch.empty(W, dtype=torch.int32, device=Q.device)
         else:
             sel, cnt = out
-        _check(lib().zha_dense_scan(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, mode, float(p), int(k),
-                                    _dev(sel, "sel"), _dev(cnt, "sel_count"), max_sel, _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_dense_scan, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq, mode,
+                float(p), int(k), _dev_of(sel, "sel", dev), _dev_of(cnt, "sel_count", dev), max_sel)
         return sel, cnt
 
     def chunk_mass(self, Q: torch.Tensor, group: int = 16, p: float = 0.9, max_sel: int | None = None, out=None,
@@ -459,8 +451,9 @@ class Tree:
             cnt = torch.empty(W, dtype=torch.int32, device=Q.device)
         else:
             sel, cnt = out
-        _check(lib().zha_chunk_mass(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, int(group), float(p),
-                                    _dev(sel, "sel"), _dev(cnt, "count"), max_sel, _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_chunk_mass, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq, int(group),
+                float(p), _dev_of(sel, "sel", dev), _dev_of(cnt, "count", dev), max_sel)
         return sel, cnt, n_chunks
 
     def ref_grad(self, Q: torch.Tensor, stream=None):
@@ -471,8 +464,9 @@ class Tree:
         B, Hq, nq, d = Q.shape
         loss = torch.empty(1, dtype=torch.float32, device=Q.device)
         grad = torch.empty(self.cfg.n_kv_heads, self.cfg.R, d, dtype=torch.float32, device=Q.device)
-        _check(lib().zha_ref_grad(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, _dev(loss, "loss"),
-                                  _dev(grad, "grad"), _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_ref_grad, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq,
+                _dev_of(loss, "loss", dev), _dev_of(grad, "grad", dev))
         return loss, grad
 
     # -- context-parallel walk (one shard of every tree per process) ------------
@@ -481,15 +475,17 @@ class Tree:
         B, Hq, nq, d = Q.shape
         counts = (ctypes.c_longlong * len(global_counts))(*[int(c) for c in global_counts])
         level = ctypes.c_int()
-        _check(lib().zha_cp_begin(self._h, _dev(Q, "Q"), _dtype_code(Q), Hq, nq, int(key_begin), counts,
-                                  len(global_counts), ctypes.byref(level), _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_cp_begin, dev, stream, self._h, _dev_of(Q, "Q", dev), _dtype_code(Q), Hq, nq, int(key_begin),
+                counts, len(global_counts), ctypes.byref(level))
         return level.value
 
     def cp_export(self, ids: torch.Tensor, scores: torch.Tensor, counts: torch.Tensor, stream=None) -> int:
         """Score this shard's frontier; ids/scores [walks][stride], counts [walks]. Returns the level."""
         level = ctypes.c_int()
-        _check(lib().zha_cp_export(self._h, _dev(ids, "ids"), _dev(scores, "scores"), _dev(counts, "counts"),
-                                   ids.shape[1], ctypes.byref(level), _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_cp_export, dev, stream, self._h, _dev_of(ids, "ids", dev), _dev_of(scores, "scores", dev),
+                _dev_of(counts, "counts", dev), ids.shape[1], ctypes.byref(level))
         return level.value
 
     def cp_select(self, ids: torch.Tensor, scores: torch.Tensor, counts: torch.Tensor, mode: int, p: float, k: int,
@@ -497,14 +493,15 @@ class Tree:
         """Choose over the gathered lists (ids/scores [parts][walks][stride], counts
         [parts][walks]); returns the next level (0 when the walk is complete)."""
         level = ctypes.c_int()
-        _check(lib().zha_cp_select(self._h, ids.shape[0], _dev(ids, "ids"), _dev(scores, "scores"),
-                                   _dev(counts, "counts"), ids.shape[2], mode, float(p), int(k), _dev(sel, "sel"),
-                                   _dev(sel_count, "sel_count"), sel.shape[1], ctypes.byref(level),
-                                   _stream(stream)))
+        dev = self._device
+        _launch(lib().zha_cp_select, dev, stream, self._h, ids.shape[0], _dev_of(ids, "ids", dev),
+                _dev_of(scores, "scores", dev), _dev_of(counts, "counts", dev), ids.shape[2], mode, float(p), int(k),
+                _dev_of(sel, "sel", dev), _dev_of(sel_count, "sel_count", dev), sel.shape[1], ctypes.byref(level))
         return level.value
 
     def reserve(self, max_walks: int, max_sel: int) -> None:
-        _check(lib().zha_reserve(self._h, int(max_walks), int(max_sel)))
+        with torch.cuda.device(self._device):
+            _check(lib().zha_reserve(self._h, int(max_walks), int(max_sel)))
 
     # -- diagnostics --------------------------------------------------------
     def profile(self, enable: bool) -> None:
@@ -512,12 +509,12 @@ class Tree:
 
     def profile_read(self, stream=None) -> dict:
         arr = (KernelTime * len(KERNEL_KINDS))()
-        _check(lib().zha_profile_read(self._h, arr, _stream(stream)))
+        _launch(lib().zha_profile_read, self._device, stream, self._h, arr)
         return {name: (arr[i].launches, arr[i].ms) for i, name in enumerate(KERNEL_KINDS)}
 
     def last_search_info(self, stream=None) -> dict:
         info = SearchInfo()
-        _check(lib().zha_last_search_info(self._h, ctypes.byref(info), _stream(stream)))
+        _launch(lib().zha_last_search_info, self._device, stream, self._h, ctypes.byref(info))
         return {"start_level": info.start_level, "union_nodes": list(info.union_nodes),
                 "walk_nodes": list(info.walk_nodes)}
 
@@ -528,7 +525,7 @@ class Tree:
         _check(lib().zha_test_wait_limit(self._h, int(wait_ns), 1 if stall else 0))
 
     def sync_status(self, stream=None) -> None:
-        _check(lib().zha_sync_status(self._h, _stream(stream)))
+        _launch(lib().zha_sync_status, self._device, stream, self._h)
 
     def close(self) -> None:
         if self._h and self._h.value:
@@ -590,10 +587,11 @@ def lse_combine(outs: torch.Tensor, lses: torch.Tensor, out_dtype=torch.float32,
     """Attention over the union of disjoint key sets: outs [parts][walks][d] fp32,
     lses [parts][walks] fp32 -> (out [walks][d] of out_dtype, lse [walks])."""
     P, W, d = outs.shape
+    dev = _cuda_index(outs, "outs")
     out = torch.empty(W, d, dtype=out_dtype, device=outs.device)
     lse = torch.empty(W, dtype=torch.float32, device=outs.device)
-    _check(lib().zha_lse_combine(P, W, d, _dev(outs, "outs"), _dev(lses, "lses"), _dev(out, "out"),
-                                 _dtype_code(out), _dev(lse, "lse"), _stream(stream)))
+    _launch(lib().zha_lse_combine, dev, stream, P, W, d, _dev_of(outs, "outs", dev), _dev_of(lses, "lses", dev),
+            _dev_of(out, "out", dev), _dtype_code(out), _dev_of(lse, "lse", dev))
     return out, lse
 
 
