@@ -307,6 +307,10 @@ int zha_attend(zha_tree *tree, const void *Q, zha_dtype q_dtype, int n_q_heads, 
  *   drafted token j. A row may be empty (padding): the token then attends to its
  *   cached keys alone, and gets out = 0, lse = -inf if it has none of those either.
  * n_draft: 1 .. ZHA_MAX_DRAFT.
+ * Roundings over an 8-bit cache are zha_attend's. Over the others, and of the drafted
+ * rows, products are of bf16 terms: one of a bf16 element and three (24 bits) of an fp32
+ * one, two (2^-17) of a weight for a bf16 out and three for an fp32 one; sums are fp32
+ * (zha_attend takes an fp32 cache's dot products in fp64).
  * out, lse: as zha_attend. A NaN among the keys and values a walk attends to
  *   gives NaN; rows it does not attend to are without effect, whatever they hold.
  * Scratch as zha_attend (zha_reserve before capturing the call in a graph). Calls on

@@ -21,10 +21,12 @@
 //              goes to scratch and combine_kernel merges the parts in order (the CTA
 //              that ends last doing it, by a ticket, took 2 to 5 us longer).
 //              The drafted tokens are more tiles, of the block's last part.
-// No atomics on results: every call gives the same bits. mma.sync and not tcgen05:
-// a gathered tile has at most 16 walks, an eighth of a tcgen05 tile's 128 rows, and
-// its accumulators never leave the warp's registers between two tiles. Keys are the
-// m side, so that 8 walks (the heads of a group) fill an instruction.
+// No atomics on results: every call gives the same bits. mma.sync and not tcgen05: a
+// decode step has 4 to 16 walks a tree, an eighth of a tcgen05 tile's 128 rows at most,
+// and accumulators that never leave the warp's registers between two tiles. Trees of more
+// walks are cut into blocks of 16 all the same, each with its own union: where their
+// selections overlap, a row is decoded once a block, and a wider block for tcgen05 would
+// decode it once. Keys are the m side, so that 8 walks (the heads of a group) fill an instruction.
 //
 // Operands. E4M3 codes are exact in fp16, so an 8-bit cache is decoded to fp16 pairs
 // in registers; exponents stay outside: 2^e of a key scales its row of S, 2^e of
@@ -48,9 +50,9 @@
 // whose sums are small beside the block's largest values (VSUM_ONE).
 //
 // Measured, 8-bit cache, d = 128, bf16, 4 heads a KV head: 256 walks of 96 chunks of 8
-// over 262,144 keys 19.4 us a call (the item kernel, a walk at a time: 39), 1,024 walks of
-// 48 chunks of 16 over 65,536 keys 26.2 us (98), 64 walks of 1,024 chunks of 16 over
-// 1,048,573 keys 46 us (145). The bytes take 3.7, 0.6 and 19.4 us at the copy rate. What
+// over 262,144 keys 19.5 us a call (the item kernel, a walk at a time: 39), 1,024 walks of
+// 48 chunks of 16 over 65,536 keys 26.3 us (98), 64 walks of 1,024 chunks of 16 over
+// 1,048,573 keys 47.5 us (145). The bytes take 3.7, 0.6 and 19.4 us at the copy rate. What
 // bounds it is latency: a CTA of the second spends 11 us on the plan, the lists, the union
 // and the merge, chains of dependent steps with barriers, and 6 on tiles; one of the third 14
 // on tiles. A tile is some 450 instructions (decoding, 32 mma.sync, the softmax, the copies)

@@ -487,9 +487,12 @@ __global__ void atc_finish_kernel(const unsigned *mkey, const float *lsum, const
 int attend_tc_walks(const zha_tree *t, long long G) {
     const zha_config &c = t->cfg;
     // chunks of 8 to 64 keys (powers of two): a tile's chunk mask fits in 16 bits. An 8-bit
-    // cache's blocks of walks take less time up to some 3,700 walks a tree (256K keys,
-    // 1,300 keys a walk: 1,008 walks 0.45 ms there and 1,024 here 1.51 ms; here 4,096 walks
-    // 1.64 ms, four times 1,008 there 1.8)
+    // cache goes to blocks of walks up to TC_E4M3_MIN_G: on the prefill workload's selections
+    // (4 trees of 262,144 keys, 1,290 keys a walk that neighbours share) 2,048 walks a tree take 0.81
+    // ms there, 4,096 take 1.58 there and 1.65 here, 8,192 take 2.89 and 1.88, 16,384 take 5.16
+    // and 2.93. The time here goes with the cache's tiles, so selections that reach many tiles with few
+    // walks each are faster in blocks at these sizes too, which G alone does not tell (random chunks:
+    // 4,096 walks of 16 keys 0.06 ms there and 1.37 here, of 1,280 keys 1.16 and 3.23).
     const int least = c.kv_dtype == ZHA_E4M3 ? TC_E4M3_MIN_G : TC_MIN_G;
     if (c.d != TC_K || c.kv_dtype == ZHA_F32 || G < least || c.chunk < 8 || c.chunk > 64 || (c.chunk & (c.chunk - 1)))
         return 0;
